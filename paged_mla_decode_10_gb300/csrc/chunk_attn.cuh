@@ -92,11 +92,19 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr int kThreads = 448;
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 384;
 #if MLA_CHUNK_F8
-// P is held as two e4m3 values, the second the rounded remainder of the first.  A row's maximum stands
-// between 2^4.5 and 2^8.5 (e4m3 ends at 448): the remainder's last place, 2^-10 at worst, is then
-// 2^-14.5 of the largest weight or less.  A smaller headroom would hold smaller weights but raise the
-// reference, and rescale O, on most tiles: with 2^7 and 2^8 (and a remainder taken in fp32) 686 us, so 559, on
-// 2 x 500 x 128 over 7.8k keys.
+// P is held as two 8-bit floats, e4m3 and the e5m2 of what that leaves.  A row's maximum stands between 2^4.5 and
+// 2^8.5 (e4m3 ends at 448).  A smaller headroom would hold smaller weights but raise the reference, and rescale O, on
+// most tiles: with 2^7 and 2^8 (and a remainder taken in fp32) 686 us, so 559, on 2 x 500 x 128 over 7.8k keys.
+//
+// Weights from 2^-6 on are held to the nearest of 8 significant bits, 2^-8 of their binade.  Smaller ones have fewer
+// (2^-14 is off at worst).  Against the row's large weights that is little for one key; but the many keys 7 nats or more
+// below a few large ones may all round the same way, while the denominator sums them as they are: 65,000 equal ones 10
+// nats down would lose 4 % of their mass, below 2^-17 all of it.  So what 8 bits leave of a remainder beyond e5m2's
+// three is rounded up or down by thresholds that take every value equally often (dithering): the 32 keys of a thread have
+// 32 thresholds evenly spread over the step, in bit-reversed order, and a byte that changes with the row and the thread's
+// keys is XORed to all.  Each weight is then right in the mean, to 2^-8 or fp16's 2^-25, and the sum over many keys to a
+// part of a step.  It costs 3 % (450 -> 462 us).  A remainder in e4m3 would end at 2^-10, 2^-14.5 of the largest weight:
+// 40,000 keys 10.5 nats below one, half of the mass, came out as 0.
 constexpr float kRescaleThreshold = 4.0f, kPExp = 4.5f;
 #else
 constexpr float kRescaleThreshold = 8.0f, kPExp = 0.0f;
@@ -386,7 +394,7 @@ __device__ void pv_role(const Ctx &c, const ChunkParams &p, ChunkWalk walk, Chun
     uint32_t it = 0, vp = 0, g = 0;   // tiles, pages, pieces
     bool ok = true;
 #if MLA_CHUNK_F8
-    constexpr uint32_t idPV = make_idesc_e4m3(128, 256, false, true);
+    constexpr uint32_t idPV = make_idesc_e4m3(128, 256, false, true), idLow = idPV | kIdescAE5m2;
 #else
     constexpr uint32_t idPV = make_idesc_bf16(128, 256, false, true);
 #endif
@@ -408,14 +416,14 @@ __device__ void pv_role(const Ctx &c, const ChunkParams &p, ChunkWalk walk, Chun
                 if (lane == 0) {
                     const uint32_t acc = t > w.lo || pg > 0 ? 1u : 0u;
 #if MLA_CHUNK_F8
-                    // P: 128 keys a row, upper parts, then lower parts 8 KB on; V: a box of 128 dims for each h
+                    // P: 128 keys a row, e4m3 parts, then e5m2 remainders 8 KB on; V: a box of 128 dims for each h
                     const uint64_t a = make_sdesc(pbuf, 16, 1024, kSwizzle128B) + 4u * pg;
                     const uint64_t b = make_sdesc(c.base + OFF_V + st * kUnitBytes + 8192u * (uint32_t)h, 8192, 1024, kSwizzle128B);
 #pragma unroll
                     for (int k = 0; k < kPage / kStepKeys; ++k) {   // +32 keys: +4096 bytes of V
                         if (k < steps) {
                             umma2_ss<1>(d, a + 2u * k, b + 256u * k, idPV, k > 0 ? 1u : acc);
-                            umma2_ss<1>(d, a + 512u + 2u * k, b + 256u * k, idPV, 1u);
+                            umma2_ss<1>(d, a + 512u + 2u * k, b + 256u * k, idLow, 1u);
                         }
                     }
 #else
@@ -532,16 +540,26 @@ __device__ __forceinline__ int ordered(float x) {
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 #if MLA_CHUNK_F8
-// Two weights as e4m3 pairs: `hi` the weights rounded, `lo` what is left, rounded.  By way of fp16, which
-// holds the weights to 2^-12 and the differences exactly.
-__device__ __forceinline__ void split_e4m3x2(float2 p, uint16_t &hi, uint16_t &lo) {
+// Two weights: `hi` as an e4m3 pair, and what is left as e5m2 in the upper byte of each half of the result.  By way of
+// fp16 (2^-11 of a weight's binade).  The remainder passes through a sum with 8 hi, which keeps 8 significant bits
+// of the weight; where hi is a normal number that leaves the remainder three, which e5m2 holds.  An fp16 value's upper
+// byte is an e5m2 value: a threshold (a byte) added to the lower one carries into it if the two pass 255.
+__device__ __forceinline__ uint32_t split_e4m3x2(float2 p, uint16_t &hi, uint32_t threshold) {
     uint32_t h, back, rest;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(p.y), "f"(p.x));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(h));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(back));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(rest) : "r"(back), "r"(0x47004700u), "r"(h));      // 8 back + (h - back)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(rest) : "r"(back), "r"(0xc800c800u), "r"(rest));   // - 8 back
+    return rest + threshold;
 }
+// Thresholds of the keys 2i and 2i + 1 of a thread's 32: 8 * (key's five bits reversed) + 4, in either half.
+__host__ __device__ constexpr uint32_t dither_of(int key) {
+    uint32_t v = 0;
+    for (int i = 0; i < 5; ++i) v |= (uint32_t)((key >> i) & 1) << (7 - i);
+    return v + 4u;
+}
+__host__ __device__ constexpr uint32_t dither_pair(int i) { return dither_of(2 * i) | dither_of(2 * i + 1) << 16; }
 #endif
 
 __device__ void softmax_role(const Ctx &c, const ChunkParams &p, ChunkWalk walk, ChunkPiece w, bool have_piece, uint32_t tmem,
@@ -618,6 +636,7 @@ __device__ void softmax_role(const Ctx &c, const ChunkParams &p, ChunkWalk walk,
             const float neg_m = m_ref == -INFINITY ? 0.f : kPExp - m_ref;
             float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #if MLA_CHUNK_F8
+            const uint32_t shift = ((uint32_t)(4 * t + 2 * kh + part + 61 * row) * 0x9e3779b1u >> 24) * 0x00010001u;
             uint32_t pk[8], pl[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -625,11 +644,11 @@ __device__ void softmax_role(const Ctx &c, const ChunkParams &p, ChunkWalk walk,
                 const float2 a23 = __ffma2_rn(make_float2(sv[4 * j + 2], sv[4 * j + 3]), make_float2(c2, c2), make_float2(neg_m, neg_m));
                 const float2 p01 = make_float2(ex2_approx(a01.x), ex2_approx(a01.y));
                 const float2 p23 = make_float2(ex2_approx(a23.x), ex2_approx(a23.y));
-                uint16_t h0, h1, l0, l1;
-                split_e4m3x2(p01, h0, l0);
-                split_e4m3x2(p23, h1, l1);
+                uint16_t h0, h1;
+                const uint32_t r0 = split_e4m3x2(p01, h0, dither_pair(2 * j) ^ shift);
+                const uint32_t r1 = split_e4m3x2(p23, h1, dither_pair(2 * j + 1) ^ shift);
                 pk[j] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-                pl[j] = (uint32_t)l0 | ((uint32_t)l1 << 16);
+                pl[j] = __byte_perm(r0, r1, 0x7531);
                 ps[0] = __fadd2_rn(ps[0], p01);
                 ps[1] = __fadd2_rn(ps[1], p23);
             }

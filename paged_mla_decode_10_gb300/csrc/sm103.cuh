@@ -259,6 +259,9 @@ __host__ __device__ constexpr uint32_t make_idesc_e4m3(uint32_t M, uint32_t N, b
          | ((M >> 4) << 24);
 }
 
+// kind::f8f6f4 takes A and B of different 8-bit types: this bit makes A e5m2 (format code 1).
+constexpr uint32_t kIdescAE5m2 = 1u << 7;
+
 // Byte offset of element (row, chunk16) inside a K-major swizzled tile whose
 // rows are `row_bytes` long (128 for SW128, 64 for SW64), as TMA writes it
 // and as the tensor core reads it: the 16-byte chunk index is XORed with the
