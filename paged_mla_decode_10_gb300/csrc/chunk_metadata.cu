@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) mla_chunk_metadata_kernel(const int3
         carry += all;
         __syncthreads();
     }
-    const long long W = line[batch];
+    const long long W = carry;   // not from shared memory: without a sequence no barrier has come since line[0] was set
     long long share = (W + parts - 1) / parts;
     if (share < kMinShare) share = kMinShare;
     // cut p lies between parts p - 1 and p
