@@ -437,6 +437,8 @@ typedef struct {
  * out_dtype.  e4m3 values are multiplied by out_scale first (1 for the other types).
  * out == x (same type and strides) rotates in place and leaves the other dims alone; otherwise
  * they are copied, and x and out must not overlap in any other way.
+ * What is written (whole rows, in place their rotated dims) must not overlap itself: of the dimensions with more
+ * than one entry, by rising stride, each steps past all that those before it span (else MLA_ERR_ARG).
  * One launch.  Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED (batch * tokens * heads above 2^31 - 1025),
  * MLA_ERR_ARCH, MLA_ERR_CUDA.
  */

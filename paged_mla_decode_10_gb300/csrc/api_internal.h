@@ -33,6 +33,23 @@ int stream_workspace(size_t need, cudaStream_t stream, void **ws, size_t *ws_byt
 int encode_map_4d(CUtensorMap *map, int elem, const void *base, const uint64_t dims[4], const uint64_t strides[3],
                   const uint32_t box[4], CUtensorMapSwizzle swizzle);
 
+// Whether rows of `extent` elements, n[i] of them at stride s[i] in each of `dims` dimensions, share no element: by rising
+// stride, each dimension of more than one entry must step past all that the ones before it span.  (Layouts that
+// interleave their dimensions without such an order are taken to overlap.)
+inline bool rows_apart(const int64_t *n, const int64_t *s, int dims, int64_t extent) {
+    __int128 span = extent;
+    for (int left = (1 << dims) - 1; left;) {
+        int k = -1;   // the dimension of the smallest stride that is left
+        for (int i = 0; i < dims; ++i)
+            if ((left >> i & 1) && (k < 0 || s[i] < s[k])) k = i;
+        left &= ~(1 << k);
+        if (n[k] <= 1) continue;
+        if (s[k] < span) return false;
+        span += (__int128)(n[k] - 1) * s[k];
+    }
+    return true;
+}
+
 inline bool is_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace mla

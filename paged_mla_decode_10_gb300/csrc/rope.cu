@@ -359,13 +359,13 @@ int mla_rope(const mla_rope_plan_t *plan, const mla_rope_shape_t *shape, const v
     if (rows > 0x7fffffffll - 1024) return report_error(MLA_ERR_UNSUPPORTED, "batch * tokens * heads exceeds 2^31 - 1025");
     if (rows == 0) return MLA_OK;
     if (!x || !out || !positions) return report_error(MLA_ERR_ARG, "NULL tensor pointer");
+    const int64_t n[3] = {sh.batch, sh.tokens, sh.heads};
+    const bool in_place = x == out;
+    // What different threads write must lie apart: whole rows, or in place their rotated dims.
+    if (!rows_apart(n, sh.out_stride, 3, in_place ? plan->rotary_dim : sh.head_dim))
+        return report_error(MLA_ERR_ARG, "out rows overlap (a stride smaller than what the others span)");
     if (!is_aligned(x, bi) || !is_aligned(out, bo) || !is_aligned(positions, 4))
         return report_error(MLA_ERR_ARG, "pointer not aligned to its element");
-    // Rows written by different threads must be different rows.
-    const int64_t n[3] = {sh.batch, sh.tokens, sh.heads};
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && sh.out_stride[i] == 0) return report_error(MLA_ERR_ARG, "out rows overlap (stride 0)");
-    const bool in_place = x == out;
     if (in_place) {
         bool same = !e4m3;
         for (int i = 0; i < 3; ++i) same = same && (n[i] == 1 || sh.x_stride[i] == sh.out_stride[i]);
