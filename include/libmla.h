@@ -475,6 +475,7 @@ typedef struct {
  * MLA_DEVERR_BAD_BLOCK.  All other cache rows stay as they are.  Two tokens that the table sends
  * to one row leave either's values.  One launch.
  * Alignment: latent and k_rope 16 bytes, caches 16 (e4m3: 8), strides multiples of 8 elements.
+ * The caches' rows must not overlap: as mla_rope's.
  * Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED (total_tokens * h_k above 2^31 - 65), MLA_ERR_ARCH,
  * MLA_ERR_CUDA.
  */
@@ -490,7 +491,8 @@ int mla_cache_append(const mla_append_shape_t *shape, const mla_rope_plan_t *pla
  *   block_table  (batch, max_blocks_per_seq) int32; bt_stride = elements per row
  *   out          (total_q, h_q, 512) bf16;   out_stride = {token, head}
  *   softmax_lse  (total_q, h_q) fp32, contiguous
- * Requirements (else MLA_ERR_ARG): as mla_shape_t's; no limit on the query rows per KV head.
+ * Requirements (else MLA_ERR_ARG): as mla_shape_t's, and the rows of out must not overlap (as mla_rope's); no limit on
+ * the query rows per KV head.
  * Limits (else MLA_ERR_UNSUPPORTED): batch <= 16384, num_parts <= 1024,
  * max_blocks_per_seq <= 2^24, total_q * h_q <= 2^31 - 1025.
  */

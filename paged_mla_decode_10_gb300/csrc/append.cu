@@ -232,10 +232,6 @@ extern "C" int mla_cache_append(const mla_append_shape_t *shape, const mla_rope_
         return report_error(MLA_ERR_ARG, "without cu_seqlens_q, total_tokens must be a multiple of batch");
     if (rows == 0 || sh.batch == 0) return MLA_OK;   // nothing, or padding only
     if (!latent || !k_rope || !block_table || !cache_seqlens || !k_cache) return report_error(MLA_ERR_ARG, "NULL tensor pointer");
-    const uintptr_t out_align = e4m3 ? 8 : 16;
-    if (!is_aligned(latent, 16) || !is_aligned(k_rope, 16) || !is_aligned(k_cache, out_align) ||
-        (krope_cache && !is_aligned(krope_cache, out_align)))
-        return report_errorf(MLA_ERR_ARG, "latent and k_rope must be 16-byte aligned, the caches %d-byte", (int)out_align);
     for (int i = 0; i < 2; ++i)
         if (sh.latent_stride[i] <= 0 || sh.latent_stride[i] % 8 || sh.k_rope_stride[i] <= 0 || sh.k_rope_stride[i] % 8)
             return report_error(MLA_ERR_ARG, "strides must be positive multiples of 8 elements");
@@ -247,6 +243,13 @@ extern "C" int mla_cache_append(const mla_append_shape_t *shape, const mla_rope_
         if (sh.k_stride[i] < dims || (krope_cache && sh.krope_stride[i] < kRope))
             return report_error(MLA_ERR_ARG, "cache strides smaller than a row");
     }
+    const int64_t n[3] = {sh.num_blocks, sh.page_block_size, sh.h_k};
+    if (!rows_apart(n, sh.k_stride, 3, dims) || (krope_cache && !rows_apart(n, sh.krope_stride, 3, kRope)))
+        return report_error(MLA_ERR_ARG, "cache rows overlap (a stride smaller than what the others span)");
+    const uintptr_t out_align = e4m3 ? 8 : 16;
+    if (!is_aligned(latent, 16) || !is_aligned(k_rope, 16) || !is_aligned(k_cache, out_align) ||
+        (krope_cache && !is_aligned(krope_cache, out_align)))
+        return report_errorf(MLA_ERR_ARG, "latent and k_rope must be 16-byte aligned, the caches %d-byte", (int)out_align);
     DeviceInfo di;
     if ((st = device_info(&di)) != MLA_OK) return st;
     AppendParams p;

@@ -51,8 +51,9 @@ int check_chunk_shape(const mla_chunk_shape_t *sh) {
     for (int i = 0; i < 3; ++i)
         if (sh->k_stride[i] <= 0 || sh->k_stride[i] % 8) return report_error(MLA_ERR_ARG, "strides must be positive multiples of 8 elements");
     // rows of out are written: they must not overlap
-    if ((sh->h_q > 1 && sh->out_stride[1] < MLA_HEAD_DIM_V) || (sh->total_q > 1 && sh->out_stride[0] < MLA_HEAD_DIM_V))
-        return report_error(MLA_ERR_ARG, "out strides smaller than a row");
+    const int64_t n[2] = {sh->total_q, sh->h_q};
+    if (!rows_apart(n, sh->out_stride, 2, MLA_HEAD_DIM_V))
+        return report_error(MLA_ERR_ARG, "out rows overlap (a stride smaller than what the other spans)");
     if (sh->bt_stride < sh->max_blocks_per_seq) return report_error(MLA_ERR_ARG, "bt_stride < max_blocks_per_seq");
     return MLA_OK;
 }

@@ -6,7 +6,7 @@ import itertools
 
 import pytest
 
-from tests.test_prefill_abi import ARG, _plan, _rope, lib  # noqa: F401
+from tests.test_prefill_abi import ARG, DUMMY, _append, _plan, _rope, _shape, lib  # noqa: F401
 
 UNALIGNED = ctypes.c_void_p(4098)
 
@@ -38,3 +38,28 @@ def test_rope_in_place_writes_the_rotated_dims_alone(lib):  # noqa: F811
         assert ARG == _rope(lib, plan, x=x, out=x, batch=1, tokens=1, heads=5, head_dim=64, rope_offset=0, strides=(0, 0, step),
                             pos=UNALIGNED)
         assert (b"aligned" if fine else b"overlap") in lib.mla_last_error(), step
+
+
+@pytest.mark.parametrize("heads, blocks, strides", [
+    (2, 3, (64 * 1152, 1152, 576)), (2, 3, (64 * 576, 576, 3 * 64 * 576)), (2, 3, (576, 2 * 3 * 576, 3 * 576)),
+    (1, 3, (64 * 640, 640, 576)), (1, 1, (576, 576, 576)), (2, 3, (64 * 1152, 576, 576)), (2, 3, (1152, 1152, 576)),
+    (2, 3, (64 * 1152 - 8, 1152, 576)), (2, 3, (64 * 1152, 1144, 576)), (1, 2, (576 * 63, 576, 576))])
+def test_append_caches(lib, heads, blocks, strides):  # noqa: F811
+    _, plan = _plan(lib)
+    fine = _apart((blocks, 64, heads), strides, 576)
+    assert ARG == _append(lib, plan, h_k=heads, num_blocks=blocks, k=strides, latent=UNALIGNED)
+    assert (b"aligned" if fine else b"overlap") in lib.mla_last_error(), lib.mla_last_error()
+    # the rotary cache of two, with the same layout in rows of 64
+    fine = _apart((blocks, 64, heads), [s // 9 // 8 * 8 for s in strides], 64)
+    assert ARG == _append(lib, plan, h_k=heads, num_blocks=blocks, kr=DUMMY, k=(64 * heads * 512, heads * 512, 512),
+                          krs=[s // 9 // 8 * 8 for s in strides], latent=UNALIGNED)
+    assert (b"aligned" if fine else b"overlap") in lib.mla_last_error(), lib.mla_last_error()
+
+
+@pytest.mark.parametrize("tokens, heads, strides", [
+    (6, 16, (16 * 512, 512)), (6, 16, (512, 6 * 512)), (1, 16, (8, 520)), (6, 1, (512, 8)), (6, 16, (16 * 520, 520)),
+    (6, 16, (512, 512)), (6, 16, (15 * 512, 512)), (6, 16, (1024, 512)), (6, 16, (512, 5 * 512)), (2, 2, (512, 512))])
+def test_chunk_out(lib, tokens, heads, strides):  # noqa: F811
+    n = ctypes.c_size_t(0)
+    rc = lib.mla_chunk_workspace_size(ctypes.byref(_shape(total_q=tokens, h_q=heads, o=strides)), ctypes.byref(n))
+    assert rc == (0 if _apart((tokens, heads), strides, 512) else ARG)
