@@ -181,6 +181,21 @@ int get_encoder(EncodeTiledFn *fn) {
     return MLA_OK;
 }
 
+// A tensor map of four dimensions, innermost first; strides in bytes of dimensions 1 to 3.  In a thread whose first CUDA
+// work this is, the driver's call, unlike the runtime's, does not make the device's context the thread's.
+CUresult encode_tiled(EncodeTiledFn enc, CUtensorMap *map, CUtensorMapDataType type, const void *base, const cuuint64_t *dims,
+                      const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    const auto encode = [&]() {
+        return enc(map, type, 4, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+    return r;
+}
+
 bool same_source(const KvSource &a, const KvSource &b) {
     return a.elem == b.elem && a.latent == b.latent && a.rope == b.rope && a.lat_dims == b.lat_dims && a.rope_dims == b.rope_dims &&
            !memcmp(a.lat_stride, b.lat_stride, sizeof a.lat_stride) &&
@@ -214,17 +229,12 @@ int kcache_maps(const mla_shape_t *sh, const KvSource &src, CUtensorMap *m128, C
                                   (cuuint64_t)src.rope_stride[0] * eb};
     // latent boxes of 128-byte rows (SW128); RoPE boxes of 32 dims: 64-byte rows (SW64) in bf16,
     // 32-byte rows (SW32) in e4m3
-    const cuuint32_t box128[4] = {(cuuint32_t)(128 / src.elem), 1, 64, 1}, box64[4] = {32, 1, 64, 1},
-                     es[4] = {1, 1, 1, 1};
+    const cuuint32_t box128[4] = {(cuuint32_t)(128 / src.elem), 1, 64, 1}, box64[4] = {32, 1, 64, 1};
     const CUtensorMapDataType dt = src.elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle rsw = src.elem == 1 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
     MapEntry &e = g_maps[g_map_next];
-    CUresult r1 = enc(&e.m128, dt, 4, const_cast<void *>(src.latent), gdim_l, gstr_l, box128, es,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    CUresult r2 = enc(&e.m64, dt, 4, const_cast<void *>(src.rope), gdim_r, gstr_r, box64, es,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, rsw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r1 = encode_tiled(enc, &e.m128, dt, src.latent, gdim_l, gstr_l, box128, CU_TENSOR_MAP_SWIZZLE_128B);
+    CUresult r2 = encode_tiled(enc, &e.m64, dt, src.rope, gdim_r, gstr_r, box64, rsw);
     if (r1 != CUDA_SUCCESS || r2 != CUDA_SUCCESS) {
         e.valid = false;
         return fail(MLA_ERR_ARG, "cache tensor map rejected by the driver (codes %d, %d): check alignment/strides",
@@ -469,17 +479,14 @@ bool query_maps(const mla_shape_t *sh, int elem, DecodeParams &p, CUtensorMap *l
     // latent boxes of 128-byte rows (SW128); RoPE boxes of 32 dims: 64-byte rows (SW64) in bf16,
     // 32-byte rows (SW32) in e4m3 -- the layouts of the Q RoPE tile the kernel keeps
     const cuuint32_t box_l[4] = {(cuuint32_t)(128 / elem), (cuuint32_t)hb, (cuuint32_t)tb, 1},
-                     box_r[4] = {32, (cuuint32_t)hbr, (cuuint32_t)tbr, 1}, es[4] = {1, 1, 1, 1};
+                     box_r[4] = {32, (cuuint32_t)hbr, (cuuint32_t)tbr, 1};
     const CUtensorMapDataType dt = elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle rsw = elem == 1 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
     QMapEntry &e = g_qmaps[g_qmap_next];
     g_qmap_next = (g_qmap_next + 1) % kMapCache;
     e.key = k;
-    CUresult r1 = enc(&e.lat, dt, 4, const_cast<void *>(k.lat), gdim_l, gstr_l, box_l, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    CUresult r2 = enc(&e.rope, dt, 4, const_cast<void *>(k.rope), gdim_r, gstr_r, box_r, es,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, rsw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r1 = encode_tiled(enc, &e.lat, dt, k.lat, gdim_l, gstr_l, box_l, CU_TENSOR_MAP_SWIZZLE_128B);
+    CUresult r2 = encode_tiled(enc, &e.rope, dt, k.rope, gdim_r, gstr_r, box_r, rsw);
     e.ok = r1 == CUDA_SUCCESS && r2 == CUDA_SUCCESS;
     e.valid = true;
     *lat = e.lat;
@@ -674,24 +681,11 @@ int encode_map_4d(CUtensorMap *map, int elem, const void *base, const uint64_t d
         if (st != MLA_OK) return st;
     }
     cuuint64_t gdim[4], gstr[3];
-    cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
+    cuuint32_t bx[4];
     for (int i = 0; i < 4; ++i) { gdim[i] = dims[i]; bx[i] = box[i]; }
     for (int i = 0; i < 3; ++i) gstr[i] = strides[i];
-    const auto encode = [&]() {
-        return enc(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                   const_cast<void *>(base), gdim, gstr, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
-    CUresult r = encode();
-    if (r == CUDA_ERROR_INVALID_CONTEXT) {
-        // a thread whose first CUDA work this is: the driver's call, unlike the runtime's, does not make the
-        // device's context the thread's
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaSetDevice(dev);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
-        r = encode();
-    }
+    const CUresult r = encode_tiled(enc, map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
+                                    gdim, gstr, bx, swizzle);
     if (r != CUDA_SUCCESS)
         return fail(MLA_ERR_ARG, "tensor map rejected by the driver (code %d): check alignment/strides", (int)r);
     return MLA_OK;
