@@ -5,6 +5,9 @@ Each function checks its tensors, marshals pointers and sizes into one C call
 (include/libmla.h) and enqueues it on the tensors' device: on ``stream``, or on
 that device's current stream.
 
+None of the calls records an autograd graph; the one whose gradient is offered, :func:`mla_rope`, refuses a tensor that
+would need it.
+
 The checks and the C structs depend on shapes, strides, types and devices alone
 ("layout"), so they are made once for each layout and kept; addresses are read at
 every call.  On the host processor of a GB300 the checks take 30 to 60 us, longer
@@ -195,9 +198,14 @@ def mla_rope(x: torch.Tensor, positions: torch.Tensor, plan: MlaRopePlan, rope_o
              out_scale: float = 1.0, stream=None) -> torch.Tensor:
     """x (..., heads, head_dim) bf16, fp16 or fp32 with ``plan.rotary_dim`` dims of every head rotated by
     positions (int32, x's shape without its last two dimensions).  The rotated dims start at
-    ``rope_offset`` (default: they are the last ones); the others are copied.  ``inverse`` rotates back, which
-    is also the gradient.  ``out``: where to write, ``x`` itself to rotate in place; ``out_dtype``
-    float8_e4m3fn rounds ``out_scale`` times the values to e4m3.  One or two leading dimensions."""
+    ``rope_offset`` (default: they are the last ones); the others are copied.  ``inverse`` turns the other way, with the
+    same factor (it rotates back where the plan's factor is 1): the gradient of a call is the inverse call on the
+    output's gradient.  The call records no graph, so that a tensor that requires one is refused while gradients are
+    enabled; make both calls in a ``torch.autograd.Function``.  ``out``: where to write, ``x`` itself to rotate in place;
+    ``out_dtype`` float8_e4m3fn rounds ``out_scale`` times the values to e4m3.  One or two leading dimensions."""
+    if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
+        raise ValueError("mla_rope records no graph: call it under torch.no_grad() or in a torch.autograd.Function, "
+                         "with inverse=True for the gradient")
     key = (_sig(x), _sig(positions), _sig(out), plan.rotary_dim, rope_offset, out_dtype)
     lay = _rope_layouts.get(key) or _rope_layout(key, x, positions, plan.rotary_dim, rope_offset, out, out_dtype)
     return _call(_rope_run, lay, stream, x, positions, plan, bool(inverse), out, float(out_scale))
