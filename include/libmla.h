@@ -296,7 +296,9 @@ int mla_decode_fwd_split(const mla_shape_t *shape, const mla_rope_strides_t *rop
  * two launches are those of mla_decode_fwd.
  *
  * Accuracy.  The probabilities are rounded to e4m3 for the PV product (the
- * denominator sums them unrounded): each weight errs by up to 2^-4 of itself.
+ * denominator sums them unrounded): each weight errs by up to 2^-4 of itself, and below 2^-6 of its
+ * row's largest by up to 2^-10 of that one, so that many keys 7 nats or more below a few others may
+ * lose their part.
  * With more than 32 query rows per KV head the two halves of each logit,
  * s_0 and s_1 (latent dims 0-255 + RoPE dims 512-543, and the rest), are
  * rounded to bf16 before they are added, which moves a logit by at most
@@ -432,9 +434,10 @@ typedef struct {
 /*
  * Rotary positions: out = x with the dims [rope_offset, rope_offset + rotary_dim) of every head
  * rotated, (a, b) -> factor * (a cos t - b sin t, b cos t + a sin t), t = position * frequency
- * (inverse != 0: -t, which is also the gradient of the forward call).  Angles are exact modulo
- * one turn for every int32 position; cos and sin are fp32; each value is rounded once, to
- * out_dtype.  e4m3 values are multiplied by out_scale first (1 for the other types).
+ * (inverse != 0: -t, which is also the gradient of the forward call; it undoes that call where factor is 1).
+ * The reduction modulo one turn is exact for every int32 position; the frequency is a 64-bit float's, which
+ * leaves an angle off by up to |position * frequency| * 2^-52; cos and sin are fp32; each value is rounded
+ * once, to out_dtype.  e4m3 values are multiplied by out_scale first (1 for the other types).
  * out == x (same type and strides) rotates in place and leaves the other dims alone; otherwise
  * they are copied, and x and out must not overlap in any other way.
  * What is written (whole rows, in place their rotated dims) must not overlap itself: of the dimensions with more
@@ -472,7 +475,8 @@ typedef struct {
  * at +-448; a bf16 one needs kv_scale == 1.  Every value is rounded once.
  * Tokens outside every sequence are padding and are skipped.  A position that is negative or past
  * the block table, or a block outside [0, num_blocks), is not stored and raises
- * MLA_DEVERR_BAD_BLOCK.  All other cache rows stay as they are.  Two tokens that the table sends
+ * MLA_DEVERR_BAD_BLOCK.  (An e4m3 cache in two tensors is for readers of the caller's own: the split calls of this
+ * library take bf16 alone.)  All other cache rows stay as they are.  Two tokens that the table sends
  * to one row leave either's values.  One launch.
  * Alignment: latent and k_rope 16 bytes, caches 16 (e4m3: 8), strides multiples of 8 elements.
  * The caches' rows must not overlap: as mla_rope's.
@@ -566,7 +570,12 @@ int mla_chunk_fwd_split(const mla_chunk_shape_t *shape, const mla_chunk_rope_str
 
 /* mla_chunk_fwd over an e4m3 query and cache, with the product scales of mla_decode_fwd_fp8
  * (logits bmm1_scale * q.k, out times bmm2_scale).  Strides of q and k_cache are multiples of 16
- * elements. */
+ * elements.
+ * Accuracy.  For the second product a softmax weight is held to 2^-8 of itself down to 2^-10.5 of its
+ * row's largest weight or less.  Smaller ones have fewer bits and are rounded up or down so that each is right in the
+ * mean to 2^-8 of itself, down to 2^-29 of the largest: a single one is off by less than a quarter of itself (or 2^-20
+ * of the largest), the sum over many by much less.  The rounding depends on the row, the key's place and the schedule
+ * alone: the same call gives the same bits.  softmax_lse has unrounded weights. */
 int mla_chunk_fwd_fp8(const mla_chunk_shape_t *shape, const void *q, const void *k_cache, const int32_t *block_table,
                       const int32_t *cu_seqlens_q, const int32_t *cache_seqlens, const int32_t *chunk_metadata,
                       float bmm1_scale, float bmm2_scale, int causal, void *out, float *softmax_lse, void *workspace,

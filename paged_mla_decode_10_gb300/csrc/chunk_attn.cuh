@@ -41,12 +41,13 @@
 // Every wait is bounded; a timeout sets MLA_DEVERR_TIMEOUT, drains copies and MMAs and returns.
 //
 // Bound by the tensor cores.  A bf16 tile is 2182 cycles of MMAs alone and takes 2470 to 2700; an e4m3 one
-// 1740 (P's remainder is a second PV product) and about 2200; between two blocks of rows pass 10000 to
+// 1740 (P's remainder is a second PV product) and about 2230; between two blocks of rows pass 10000 to
 // 12000 cycles without products (last weights -> last PV -> next Q -> output -> first weights).  Tensor pipe
-// active 74 % (bf16) and 78 % (e4m3) of 512 x 128 rows over 6k keys.  Measured: 1024 x 128 rows over 15k keys 2.45 to
-// 2.5 ms (1760 to 1809 TFLOP/s; the power limit lowers the clock), 24 ragged sequences with 23 decoding 313 us
-// (1300), 61 x 16 rows over 65k keys 119 us (1160; their keys come from HBM, 1.8 times, and tiles of the farther die
-// take 10 % longer), e4m3 2 x 500 x 128 rows over up to 7.8k keys 450 us (2150), 17 x 16 rows over 300 keys 20 us.
+// active 74 % (bf16) and 75 % (e4m3) of 512 x 128 rows over 6k keys.  Measured with both launches, single calls between
+// pauses: 1024 x 128 rows over 15k keys 2.45 to 2.5 ms (1760 to 1809 TFLOP/s; one after another 2.75 ms, 1610, as the
+// power limit lowers the clock), 24 ragged sequences with 23 decoding 313 us (1300), 61 x 16 rows over 65k keys 117 us
+// (1180; their keys come from HBM, 1.8 times, and tiles of the farther die take 10 % longer), e4m3 2 x 500 x 128 rows
+// over up to 7.8k keys 457 to 465 us (2100; one after another 500, 1940), 17 x 16 rows over 300 keys 20 us.
 
 namespace mla {
 namespace MLA_CHUNK_NS {
@@ -103,8 +104,8 @@ constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 384;
 // three is rounded up or down by thresholds that take every value equally often (dithering): the 32 keys of a thread have
 // 32 thresholds evenly spread over the step, in bit-reversed order, and a byte that changes with the row and the thread's
 // keys is XORed to all.  Each weight is then right in the mean, to 2^-8 or fp16's 2^-25, and the sum over many keys to a
-// part of a step.  It costs 3 % (450 -> 462 us).  A remainder in e4m3 would end at 2^-10, 2^-14.5 of the largest weight:
-// 40,000 keys 10.5 nats below one, half of the mass, came out as 0.
+// part of a step.  It costs 3 % (450 -> 462 us on 2 x 500 x 128 rows).  A remainder in e4m3 would end at 2^-10,
+// 2^-14.5 of the largest weight: 40,000 keys 10.5 nats below one, half of the mass, came out as 0.
 constexpr float kRescaleThreshold = 4.0f, kPExp = 4.5f;
 #else
 constexpr float kRescaleThreshold = 8.0f, kPExp = 0.0f;
@@ -147,7 +148,10 @@ __device__ void drain_after_abort() {
 
 // Arrival on CTA 0's barrier for data that this CTA's threads left in this CTA's shared memory or TMEM
 // and that this SM's tensor core reads: the threads' fences (proxy, tcgen05) order the data before it
-// within the SM, so it releases at CTA scope (at cluster scope it held its warp up for 1350 cycles).
+// within the SM, so it releases at CTA scope.  That argues from the machine: the PTX memory model gives a release at
+// CTA scope no effect on a thread of the other CTA, which issues the product.  At cluster scope each arrival held its
+// warp up for 1350 cycles (311 -> 423 us on 24 ragged sequences, e4m3 463 -> 719 on 2 x 500 x 128 rows); by way of one
+// warp of CTA 1 that passes its CTA's arrivals on at cluster scope they took 323 and 487.
 __device__ __forceinline__ void mbar_arrive_lead(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
 }

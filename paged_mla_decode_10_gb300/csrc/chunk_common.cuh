@@ -18,7 +18,8 @@ constexpr int kTileKeys = 128;          // keys of a tile: two cache pages
 constexpr int kTilePages = kTileKeys / kPage;
 constexpr int kBlockRows = 128;         // query rows of a block
 constexpr int kSlotsPerPart = 2;        // partials a part can leave: of its first and of its last block
-// Fixed work of opening a block (query load, pipeline fill, output), in tiles.
+// Fixed work of opening a block (query load, pipeline fill, output), in tiles: an estimate.  A change of block was
+// measured since at 4 to 4.5 tiles' time in bf16 and 4.5 to 5.5 in e4m3; other values have not been timed.
 constexpr int kBlockCost = 3;
 // A part takes at least this much work, and a cut leaves at least kMinPiece tiles on either side:
 // splitting a block costs a second block's fixed work and the partials' way through memory.

@@ -5,7 +5,7 @@
 // (p = 10^6 and f = 1 leave 0.06 rad), and 64-bit floats are slow here.  The
 // plan therefore holds f_i / 2 pi as a 64-bit fraction of a turn: the product
 // with the position, taken modulo 2^64, is the angle modulo one turn exactly,
-// for any 32-bit position, in integer arithmetic.  Read as a signed number it
+// for any 32-bit position, in integer arithmetic (f_i itself is a 64-bit float's).  Read as a signed number it
 // lies in [-1/2, 1/2) turns and is rounded once to 32 bits.
 #pragma once
 
