@@ -640,7 +640,7 @@ __device__ void softmax_role(const Ctx &c, const ChunkParams &p, ChunkWalk walk,
             const float neg_m = m_ref == -INFINITY ? 0.f : kPExp - m_ref;
             float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #if MLA_CHUNK_F8
-            const uint32_t shift = ((uint32_t)(4 * t + 2 * kh + part + 61 * row) * 0x9e3779b1u >> 24) * 0x00010001u;
+            const uint32_t shift = ((4u * (uint32_t)t + (uint32_t)(2 * kh + part) + 61u * (uint32_t)row) * 0x9e3779b1u >> 24) * 0x00010001u;
             uint32_t pk[8], pl[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
