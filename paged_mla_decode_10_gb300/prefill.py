@@ -203,7 +203,7 @@ def mla_rope(x: torch.Tensor, positions: torch.Tensor, plan: MlaRopePlan, rope_o
     output's gradient.  The call records no graph, so that a tensor that requires one is refused while gradients are
     enabled; make both calls in a ``torch.autograd.Function``.  ``out``: where to write, ``x`` itself to rotate in place;
     ``out_dtype`` float8_e4m3fn rounds ``out_scale`` times the values to e4m3.  One or two leading dimensions."""
-    if torch.is_grad_enabled() and (x.requires_grad or (out is not None and out.requires_grad)):
+    if (x.requires_grad or (out is not None and out.requires_grad)) and torch.is_grad_enabled():
         raise ValueError("mla_rope records no graph: call it under torch.no_grad() or in a torch.autograd.Function, "
                          "with inverse=True for the gradient")
     key = (_sig(x), _sig(positions), _sig(out), plan.rotary_dim, rope_offset, out_dtype)
